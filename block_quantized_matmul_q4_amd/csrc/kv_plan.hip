@@ -136,31 +136,29 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(KvPlanArgs a, int shift)
         __syncthreads();
         const int64_t taken_now = taken_all;
         const int64_t upto_taken = upto.ask < taken_now ? upto.ask : taken_now;
-        const int takes = (int)(taken_now - taken);
+        const unsigned takes = (unsigned)(taken_now - taken);    // at most count
         take_end[tid] = (int32_t)(upto_taken - taken);
         back_end[tid] = capped(upto.back - carry.back);
         row_end[tid] = capped(upto.grow - carry.grow);
         __syncthreads();
-        for (int i = tid; i < takes; i += kThreads) {
-            const int r = upper(take_end, kThreads, i);
-            const int nth = i - (r ? take_end[r - 1] : 0);
+        for (unsigned i = tid; i < takes; i += kThreads) {
+            const int r = upper(take_end, kThreads, (int)i);
+            const int nth = (int)i - (r ? take_end[r - 1] : 0);
             a.table[(int64_t)(b0 + r) * a.width + req[r].have + nth] =
                 a.ring[wrapped(head + taken + i, size)];
         }
         // places of the ring that are free (the pages taken are still in theirs)
-        const int64_t room = size - count - carry.back;
-        const int backs = capped(total.back < room ? total.back : room);
-        for (int i = tid; i < backs; i += kThreads) {
-            const int r = upper(back_end, kThreads, i);
-            const int nth = i - (r ? back_end[r - 1] : 0);
+        const unsigned backs = kv_fitting(total.back, size - count - carry.back);
+        for (unsigned i = tid; i < backs; i += kThreads) {
+            const int r = upper(back_end, kThreads, (int)i);
+            const int nth = (int)i - (r ? back_end[r - 1] : 0);
             a.ring[wrapped(head + count + carry.back + i, size)] =
                 a.table[(int64_t)(b0 + r) * a.width + req[r].need + nth];
         }
         if constexpr (FILL) {
-            const int64_t left = a.tokens - carry.grow;
-            const int rows = (int)(total.grow < left ? total.grow : left);
+            const int rows = kv_fitting(total.grow, a.tokens - carry.grow);
             for (int i = tid; i < rows; i += kThreads) {
-                const int row = (int)carry.grow + i;
+                const int row = (int)carry.grow + i;    // below T: there are rows left
                 const int r = upper(row_end, kThreads, i);
                 const Request q = req[r];
                 int64_t slot = -1;

@@ -65,6 +65,15 @@ __host__ __device__ inline bool kv_page_exists(int page, int num_pages)
     return (unsigned)page < (unsigned)num_pages;
 }
 
+// As many of n rows or pages as there is room for. Both are sums over lengths
+// that the device holds, up to 2^52, and room is negative once more has been
+// asked for than there is; only what is left of them is narrowed.
+__host__ __device__ inline int kv_fitting(int64_t n, int64_t room)
+{
+    const int64_t most = n < room ? n : room;
+    return (int)(most < 0 ? 0 : most < INT32_MAX ? most : INT32_MAX);
+}
+
 struct KvPlanArgs {
     const int32_t *want, *lens;
     int32_t *table, *ring;

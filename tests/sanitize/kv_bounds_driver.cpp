@@ -1,0 +1,52 @@
+// Runs the index arithmetic that the kernels of the paged KV cache share
+// (csrc/qmm_kv.h) on the host, built with AddressSanitizer and
+// UndefinedBehaviorSanitizer, over sums and lengths next to and past the ends of
+// 32 bits. Exits non-zero on the first failed check.
+#include <climits>
+#include <cstdint>
+#include <cstdio>
+#include <cstdlib>
+#include <vector>
+
+#include "../../block_quantized_matmul_q4_amd/csrc/qmm_kv.h"
+
+namespace {
+long g_checks = 0;
+
+#define CHECK(cond)                                                              \
+    do {                                                                         \
+        ++g_checks;                                                              \
+        if (!(cond)) {                                                           \
+            std::fprintf(stderr, "FAILED %s:%d: %s\n", __FILE__, __LINE__, #cond); \
+            std::exit(1);                                                        \
+        }                                                                        \
+    } while (0)
+
+// Rows (pages) that a plan writes at `before`, the sum of all earlier ones, into
+// an array of `size`.
+void fitting()
+{
+    std::vector<int64_t> sums = {0, 1, 7, 1023, 1024};
+    for (int64_t at : {(int64_t)1 << 12, (int64_t)1 << 31, (int64_t)1 << 32, (int64_t)1 << 33,
+                       (int64_t)3 << 31, (int64_t)1024 * 4194303, (int64_t)1024 * 3000000,
+                       (int64_t)1 << 52})
+        for (int64_t d : {-4096, -11, -10, -1, 0, 1, 9, 10, 4096}) sums.push_back(at + d);
+    for (int64_t size : {(int64_t)0, (int64_t)1, (int64_t)10, (int64_t)4096, (int64_t)INT_MAX})
+        for (int64_t before : sums)
+            for (int64_t n : sums) {
+                const int got = qmm::kv_fitting(n, size - before);
+                CHECK(got >= 0 && got <= n);
+                CHECK(got == 0 || before + got <= size);
+                // all of them, or all that there is room for
+                CHECK(got == n || before + got == size || before >= size);
+            }
+}
+
+}  // namespace
+
+int main()
+{
+    fitting();
+    std::printf("kv bounds passed (%ld)\n", g_checks);
+    return 0;
+}
