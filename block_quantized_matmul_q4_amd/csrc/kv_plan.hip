@@ -76,11 +76,6 @@ __device__ __forceinline__ int upper(const T *a, int n, T x)
     return lo;
 }
 
-__device__ __forceinline__ int wrapped(int64_t i, int size)
-{
-    return (int)(i >= size ? i - size : i);
-}
-
 struct Request {
     int32_t lens;
     int32_t have;           // pages before the step
@@ -145,14 +140,14 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(KvPlanArgs a, int shift)
             const int r = upper(take_end, kThreads, (int)i);
             const int nth = (int)i - (r ? take_end[r - 1] : 0);
             a.table[(int64_t)(b0 + r) * a.width + req[r].have + nth] =
-                a.ring[wrapped(head + taken + i, size)];
+                a.ring[kv_ring_place(head, taken + i, size)];
         }
         // places of the ring that are free (the pages taken are still in theirs)
         const unsigned backs = kv_fitting(total.back, size - count - carry.back);
         for (unsigned i = tid; i < backs; i += kThreads) {
             const int r = upper(back_end, kThreads, (int)i);
             const int nth = (int)i - (r ? back_end[r - 1] : 0);
-            a.ring[wrapped(head + count + carry.back + i, size)] =
+            a.ring[kv_ring_place(head, count + carry.back + i, size)] =
                 a.table[(int64_t)(b0 + r) * a.width + req[r].need + nth];
         }
         if constexpr (FILL) {
@@ -169,8 +164,8 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(KvPlanArgs a, int shift)
                     const int page =
                         at < q.have
                             ? a.table[(int64_t)(b0 + r) * a.width + at]
-                            : a.ring[wrapped(head + taken + (r ? take_end[r - 1] : 0) + at - q.have,
-                                             size)];
+                            : a.ring[kv_ring_place(
+                                  head, taken + (r ? take_end[r - 1] : 0) + at - q.have, size)];
                     slot = (int64_t)page * (1 << shift) + (pos & mask);
                 }
                 a.slots[row] = slot;
@@ -188,7 +183,7 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(KvPlanArgs a, int shift)
         }
     if (tid == 0) {
         const int64_t room = size - count;
-        a.new_pool[0] = wrapped(head + taken, size);
+        a.new_pool[0] = kv_ring_place(head, taken, size);
         a.new_pool[1] = count - taken + (carry.back < room ? carry.back : room);
     }
 }

@@ -74,6 +74,14 @@ __host__ __device__ inline int kv_fitting(int64_t n, int64_t room)
     return (int)(most < 0 ? 0 : most < INT32_MAX ? most : INT32_MAX);
 }
 
+// The place `after` entries behind a ring's head, head and after at most `size`
+// (together past 32 bits in a ring of more than 2^30).
+__host__ __device__ inline int kv_ring_place(int head, int64_t after, int size)
+{
+    const int64_t at = head + after;
+    return (int)(at >= size ? at - size : at);
+}
+
 struct KvPlanArgs {
     const int32_t *want, *lens;
     int32_t *table, *ring;

@@ -42,11 +42,23 @@ void fitting()
             }
 }
 
+// Places of a ring, also of one whose head and count add up to more than 2^31.
+void ring_places()
+{
+    for (int size : {1, 2, 50, 1 << 30, (1 << 30) + 7, INT_MAX})
+        for (int head : {0, 1, size / 2, size - 1})
+            for (int64_t after : {(int64_t)0, (int64_t)1, (int64_t)size / 2, (int64_t)size - 1, (int64_t)size}) {
+                if (head >= size || after > size) continue;
+                CHECK(qmm::kv_ring_place(head, after, size) == (head + after) % size);
+            }
+}
+
 }  // namespace
 
 int main()
 {
     fitting();
+    ring_places();
     std::printf("kv bounds passed (%ld)\n", g_checks);
     return 0;
 }

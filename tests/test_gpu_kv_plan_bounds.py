@@ -71,3 +71,21 @@ def test_pages_given_back_pass_32_bits():
     assert ring.tolist() == [*range(7), *range(100, 105), *range(12, 20)]
     assert step.pool.tolist() == [12, 20] and not step.status.any() and not step.lens.any()
     assert not step.cu.any() and (step.slots == -1).all()
+
+
+def test_ring_of_more_than_2_to_the_30():
+    """Head and count add up to more than 2^31 (a ring of 6 GiB)."""
+    size, page = 3 << 29, 16
+    ring_all, ring = guarded(size, torch.int32)
+    head, count = size - 2, size - 3
+    ring.fill_(9)
+    ring[-2:] = torch.tensor([50, 51], device="cuda")
+    ring[:2] = torch.tensor([52, 53], device="cuda")
+    table = torch.tensor([[0, 0, 0], [3, 4, 5]], dtype=torch.int32, device="cuda")
+    lens = torch.tensor([0, 40], dtype=torch.int32, device="cuda")
+    want = torch.tensor([48, 10], dtype=torch.int32, device="cuda")
+    step = qmm.kv_plan(want, lens, table, ring, torch.tensor([head, count], device="cuda"), 48, page)
+    assert table.tolist() == [[50, 51, 52], [3, 4, 5]] and step.pool.tolist() == [1, count - 1]
+    end = (head + count) % size
+    assert ring[end:end + 2].tolist() == [4, 5] and int((ring[2:end] != 9).sum()) == 0
+    assert int((ring[end + 2:-2] != 9).sum()) == 0 and untouched(ring_all)
