@@ -218,7 +218,7 @@ hipError_t launch_kv_plan(const KvPlanArgs &a, hipStream_t stream)
     }
     plan_kernel<false><<<1, kThreads, 0, stream>>>(a, shift);
     if (hipError_t err = hipGetLastError()) return err;
-    fill_kernel<<<(a.tokens + 255) / 256, 256, 0, stream>>>(a, shift);
+    fill_kernel<<<kv_groups(a.tokens, 256), 256, 0, stream>>>(a, shift);
     return hipGetLastError();
 }
 

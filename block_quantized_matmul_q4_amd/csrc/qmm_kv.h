@@ -82,6 +82,12 @@ __host__ __device__ inline int kv_ring_place(int head, int64_t after, int size)
     return (int)(at >= size ? at - size : at);
 }
 
+// Workgroups of `threads` for n items, n up to 2^31 - 1.
+__host__ __device__ inline unsigned kv_groups(int n, int threads)
+{
+    return ((unsigned)n + (unsigned)threads - 1) / (unsigned)threads;
+}
+
 struct KvPlanArgs {
     const int32_t *want, *lens;
     int32_t *table, *ring;

@@ -53,11 +53,23 @@ void ring_places()
             }
 }
 
+// Workgroups for up to 2^31 - 1 rows, whose last thread still has a 32-bit number.
+void groups()
+{
+    for (int threads : {64, 256, 512, 1024})
+        for (int64_t n : {(int64_t)0, (int64_t)1, (int64_t)255, (int64_t)256, (int64_t)257,
+                          (int64_t)INT_MAX - 256, (int64_t)INT_MAX - 255, (int64_t)INT_MAX}) {
+            const int64_t got = qmm::kv_groups((int)n, threads);
+            CHECK(got == (n + threads - 1) / threads && got * threads - 1 <= INT_MAX);
+        }
+}
+
 }  // namespace
 
 int main()
 {
     fitting();
+    groups();
     ring_places();
     std::printf("kv bounds passed (%ld)\n", g_checks);
     return 0;

@@ -1,0 +1,37 @@
+"""Attention whose keys are shared out over parts: what a row gets may not depend on how
+many parts there are. Tolerances are those of test_gpu_kv.py."""
+
+import numpy as np
+import pytest
+import torch
+
+import block_quantized_matmul_q4_amd as qmm
+import kv_reference as ref
+from test_gpu_kv import Setup, device, gpu  # noqa: F401  (device: a fixture)
+
+pytestmark = pytest.mark.gpu
+
+# tokens of a request whose keys make one part, a few, and more than 16 (256 keys each)
+PARTS = [1000, 3000, 6000]
+
+
+@pytest.mark.parametrize("keys", PARTS)
+@pytest.mark.parametrize("new", [1, 40])
+def test_visible_nan_far_below_the_maximum(keys, new):
+    """A value that is NaN reaches its rows although another part's scores are so much higher
+    that its own weight underflows to 0 (0 times NaN)."""
+    s = Setup([keys], [new], 1, 1, 64, 16)
+    s.q[:] = s.q[0]
+    scale = 64 ** -0.5
+    s.scales("k", 0, 100, 0, 300.0)
+    page, place = s.tokens(0, 100)
+    k, _ = ref.get(s.cache[page, 0], 16, 64)
+    if k[place] @ s.q[0, 0] < 0:
+        s.scales("k", 0, 100, 0, -300.0)
+    # both far above exp2's underflow, for the token and for the largest of the others
+    score = abs(scale * (k[place] @ s.q[0, 0]))
+    others = 4 * 8 * np.linalg.norm(s.q[0, 0]) * scale          # scales are 0.22 on average
+    assert score > others + 200
+    s.scales("v", 0, keys - 80, 0, [0.1, np.nan])
+    o, lse = s.check(max_q=new)
+    assert np.isnan(o[..., 32:]).all() and np.isfinite(o[..., :32]).all() and np.isfinite(lse).all()

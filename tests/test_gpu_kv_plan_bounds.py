@@ -89,3 +89,17 @@ def test_ring_of_more_than_2_to_the_30():
     end = (head + count) % size
     assert ring[end:end + 2].tolist() == [4, 5] and int((ring[2:end] != 9).sum()) == 0
     assert int((ring[end + 2:-2] != 9).sum()) == 0 and untouched(ring_all)
+
+
+@pytest.mark.parametrize("tokens", [2**31 - 1, 2**31 - 256])
+def test_the_largest_number_of_rows(tokens):
+    """The rows' workgroups are counted past 2^31 (24 GiB of slots and positions)."""
+    lens = torch.tensor([20, 0], dtype=torch.int32, device="cuda")
+    want = torch.tensor([25, 1], dtype=torch.int32, device="cuda")
+    table = torch.tensor([[7, 3], [0, 0]], dtype=torch.int32, device="cuda")
+    ring = torch.tensor([8], dtype=torch.int32, device="cuda")
+    step = qmm.kv_plan(want, lens, table, ring, torch.tensor([0, 1], device="cuda"), tokens, 16)
+    assert step.slots[:6].tolist() == [3 * 16 + 4 + i for i in range(5)] + [8 * 16]
+    assert step.positions[:6].tolist() == [20, 21, 22, 23, 24, 0]
+    for x in (step.slots, step.positions):
+        assert len(x) == tokens and all((part == -1).all() for part in x[6:].split(1 << 28))
