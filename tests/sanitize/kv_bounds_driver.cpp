@@ -1,5 +1,5 @@
 // Runs the index arithmetic that the kernels of the paged KV cache share
-// (csrc/qmm_kv.h) on the host, built with AddressSanitizer and
+// (csrc/qmm_kv.h, csrc/qmm_attend_rows.h) on the host, built with AddressSanitizer and
 // UndefinedBehaviorSanitizer, over sums and lengths next to and past the ends of
 // 32 bits. Exits non-zero on the first failed check.
 #include <climits>
@@ -8,6 +8,7 @@
 #include <cstdlib>
 #include <vector>
 
+#include "../../block_quantized_matmul_q4_amd/csrc/qmm_attend_rows.h"
 #include "../../block_quantized_matmul_q4_amd/csrc/qmm_kv.h"
 
 namespace {
@@ -64,11 +65,38 @@ void groups()
         }
 }
 
+// The keys that a row sees, by the definition in 64 bits: j <= p if causal, j > p -
+// window if there is one, 0 <= j < len.
+void visible_keys()
+{
+    const int most = INT_MAX - 15;
+    for (int len : {0, 1, 3, 50, 300, most})
+        for (int count : {1, 5, 70, 1000, most})
+            for (int causal : {0, 1})
+                for (int window : {0, 1, 5, 299, INT_MAX - 50, INT_MAX - 2, INT_MAX}) {
+                    qmm::AttendArgs a = {};
+                    a.group = 1;
+                    a.causal = causal;
+                    a.window = window;
+                    const qmm::Rows rows(a, {0, count, len});
+                    for (int64_t token : {(int64_t)0, (int64_t)1, (int64_t)4, (int64_t)69,
+                                          (int64_t)count - 51, (int64_t)count - 2, (int64_t)count - 1}) {
+                        if (token < 0 || token >= count) continue;
+                        const int64_t p = (int64_t)len - count + token;
+                        int64_t lo = 0, hi = len;
+                        if (causal && p + 1 < hi) hi = p + 1 > 0 ? p + 1 : 0;
+                        if (window && p - window + 1 > 0) lo = p - window + 1;
+                        CHECK(rows.begin((int)token) == lo && rows.end((int)token) == hi);
+                    }
+                }
+}
+
 }  // namespace
 
 int main()
 {
     fitting();
+    visible_keys();
     groups();
     ring_places();
     std::printf("kv bounds passed (%ld)\n", g_checks);
