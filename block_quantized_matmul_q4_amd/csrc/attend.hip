@@ -419,9 +419,10 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttendArgs a)
     __syncthreads();
 #pragma unroll
     for (int w = 0; w < kJoinThreads / 64; ++w) m = fmaxf(m, s_wave[w]);
-    // a part that has seen nothing has l = 0 and is left out
+    // A part that has seen nothing has l = 0 and is left out, by a weight below 0: one
+    // whose weight is 0 because its scores are far lower has to bring its NaNs.
     for (int s = tid; s < a.splits; s += kJoinThreads) {
-        const float w = s_l[s] == 0.0f ? 0.0f : weight(s_w[s], m);
+        const float w = s_l[s] == 0.0f ? -1.0f : weight(s_w[s], m);
         s_w[s] = w;
         s_l[s] *= w;
     }
@@ -433,7 +434,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttendArgs a)
 #pragma unroll 8
         for (int s = group; s < a.splits; s += groups) {
             const f32x4 o = *(const f32x4 *)(a.part_o + (s * rows_all + row) * D + c);
-            if (s_l[s] != 0.0f) sum += s_w[s] * o;
+            if (!(s_w[s] < 0.0f)) sum += s_w[s] * o;
         }
     s_o[tid] = sum;
     float l = 0.0f;
