@@ -106,12 +106,12 @@ __global__ void __launch_bounds__(WAVES * 64, (kWavesPerSimd<NB, PACK, WAVES>)) 
         const Reach reach = rows_of.reach(tile * kRows, kRows);
         const auto [from, to] = part_of(reach, split, a.splits, a.min_part, kStep);
 
-        int t0 = from + wave * kKeys;
+        unsigned t0 = from + wave * kKeys;
         Half<NB> kx[2], vx[2];
         Pages pages = {{-1, -1}}, entries = {{-1, -1}};    // of the next step
         if (t0 < to) {
             pages = keys.pages(keys.look_up(t0));
-            entries = keys.look_up(to - t0 > kStep ? t0 + kStep : t0);
+            entries = keys.look_up(step_after(t0, to, kStep));
 #pragma unroll
             for (int h = 0; h < 2; ++h) keys.load_k(kx[h], pages.at[h], t0 + 16 * h);
 #pragma unroll
@@ -141,9 +141,9 @@ __global__ void __launch_bounds__(WAVES * 64, (kWavesPerSimd<NB, PACK, WAVES>)) 
         for (; t0 < to; t0 += kStep) {
             // the last step loads its own keys again, which costs less than the
             // registers that loads under a condition take
-            const int next = t0 + kStep < to ? t0 + kStep : t0;
+            const unsigned next = step_after(t0, to, kStep);
             const Pages next_pages = keys.pages(entries);
-            entries = keys.look_up(to - next > kStep ? next + kStep : next);
+            entries = keys.look_up(step_after(next, to, kStep));
 
             f32x4 s[2] = {};
 #pragma unroll
@@ -176,8 +176,8 @@ __global__ void __launch_bounds__(WAVES * 64, (kWavesPerSimd<NB, PACK, WAVES>)) 
 #pragma unroll
                     for (int r = 0; r < 4; ++r) s[h][r] += dpp_f<0x128, 0xF>(s[h][r]);
 
-            const bool whole = pages.at[0] >= 0 && pages.at[1] >= 0 && t0 >= reach.all_lo &&
-                               t0 + kKeys <= reach.all_hi && t0 + kKeys <= to;
+            const bool whole = pages.at[0] >= 0 && pages.at[1] >= 0 && t0 >= (unsigned)reach.all_lo &&
+                               t0 + kKeys <= (unsigned)reach.all_hi && t0 + kKeys <= to;
             uint32_t seen = 0xFF;               // bit 4 h + r: key 16 h + 4 g + r is visible
             if (!whole) {
                 keep_branch();
@@ -186,8 +186,8 @@ __global__ void __launch_bounds__(WAVES * 64, (kWavesPerSimd<NB, PACK, WAVES>)) 
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
-                        const int t = t0 + 16 * h + 4 * g + r;
-                        const bool ok = pages.at[h] >= 0 && t >= lo && t < min(hi, to);
+                        const int t = (int)t0 + 16 * h + 4 * g + r;
+                        const bool ok = pages.at[h] >= 0 && t >= lo && t < min(hi, (int)to);
                         seen |= (uint32_t)ok << (4 * h + r);
                         s[h][r] = ok ? s[h][r] : kNone;
                     }

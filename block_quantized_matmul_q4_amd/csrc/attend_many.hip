@@ -91,19 +91,19 @@ __global__ void __launch_bounds__(kWaves * 64, 2) attend_many_kernel(AttendArgs 
             const int row = min(tile * kRows + 16 * t + n, rows - 1);
             const int token = row / a.group, head = kvh * a.group + row % a.group;
             lo[t] = rows_of.begin(token);
-            hi[t] = min(rows_of.end(token), to);
+            hi[t] = min(rows_of.end(token), (int)to);
             q[t].load(a.q + (int64_t)(q0 + token) * a.q_stride + head * D, g, a.scale, -1.0f);
             m[t] = kLowest;
             l[t] = 0.0f;
             poison[t] = 0;
         }
 
-        int t0 = from + wave * kKeys;
+        unsigned t0 = from + wave * kKeys;
         Half<NB> kx[2], vx[2];
         Pages pages = {{-1, -1}}, entries = {{-1, -1}};    // of the next step
         if (t0 < to) {
             pages = keys.pages(keys.look_up(t0));
-            entries = keys.look_up(to - t0 > kStep ? t0 + kStep : t0);
+            entries = keys.look_up(step_after(t0, to, kStep));
 #pragma unroll
             for (int h = 0; h < 2; ++h) keys.load_k(kx[h], pages.at[h], t0 + 16 * h);
 #pragma unroll
@@ -113,9 +113,9 @@ __global__ void __launch_bounds__(kWaves * 64, 2) attend_many_kernel(AttendArgs 
         for (; t0 < to; t0 += kStep) {
             // the last step loads its own keys again, which costs less than the
             // registers that loads under a condition take
-            const int next = t0 + kStep < to ? t0 + kStep : t0;
+            const unsigned next = step_after(t0, to, kStep);
             const Pages next_pages = keys.pages(entries);
-            entries = keys.look_up(to - next > kStep ? next + kStep : next);
+            entries = keys.look_up(step_after(next, to, kStep));
 
             f32x4 s[QT][2] = {};
 #pragma unroll
@@ -141,8 +141,8 @@ __global__ void __launch_bounds__(kWaves * 64, 2) attend_many_kernel(AttendArgs 
 #pragma unroll
             for (int h = 0; h < 2; ++h) keys.load_k(kx[h], next_pages.at[h], next + 16 * h);
 
-            const bool whole = pages.at[0] >= 0 && pages.at[1] >= 0 && t0 >= reach.all_lo &&
-                               t0 + kKeys <= reach.all_hi && t0 + kKeys <= to;
+            const bool whole = pages.at[0] >= 0 && pages.at[1] >= 0 && t0 >= (unsigned)reach.all_lo &&
+                               t0 + kKeys <= (unsigned)reach.all_hi && t0 + kKeys <= to;
             uint32_t seen[QT];                  // bit 4 h + r: key 16 h + 4 g + r is visible
 #pragma unroll
             for (int t = 0; t < QT; ++t) seen[t] = 0xFF;
@@ -155,7 +155,7 @@ __global__ void __launch_bounds__(kWaves * 64, 2) attend_many_kernel(AttendArgs 
                     for (int h = 0; h < 2; ++h)
 #pragma unroll
                         for (int r = 0; r < 4; ++r) {
-                            const int at = t0 + 16 * h + 4 * g + r;
+                            const int at = (int)t0 + 16 * h + 4 * g + r;
                             const bool ok = pages.at[h] >= 0 && at >= lo[t] && at < hi[t];
                             seen[t] |= (uint32_t)ok << (4 * h + r);
                             s[t][h][r] = ok ? s[t][h][r] : kNone;

@@ -54,20 +54,32 @@ __host__ __device__ __forceinline__ int unit_of(unsigned id, int units)
 }
 
 // The part of a tile's keys that split `split` of `splits` takes, in steps of
-// `step` keys from a multiple of 32 on.
+// `step` keys from a multiple of 32 on. Places are unsigned here: a wave's next
+// step may start past 2^31 - 1, where it ends.
 struct Part {
-    int from, to;
+    unsigned from, to;
 };
 
-__host__ __device__ __forceinline__ Part part_of(const Reach &r, int split, int splits, int min_part, int step)
+__host__ __device__ __forceinline__ Part part_of(const Reach &r, int split, int splits, int min_part,
+                                                 int step)
 {
     const int start = r.lo & ~(kKeys - 1);
-    const int span = max(r.hi - start, 0);
-    const int part = max((span + splits - 1) / splits, min_part);
-    const int64_t keys = ((int64_t)part + step - 1) / step * step;
-    const int64_t from = start + keys * split;
-    const int to = (int)min((int64_t)r.hi, from + keys);
-    return {(int)min(from, (int64_t)to), to};
+    const unsigned span = max(r.hi - start, 0);
+    const unsigned each = (span + (unsigned)splits - 1) / (unsigned)splits;
+    const unsigned part = each > (unsigned)min_part ? each : (unsigned)min_part;
+    const unsigned keys = (part + step - 1) / step * step;      // at most 2^31
+    // (from the end backwards, so that no sum passes 32 bits)
+    const uint64_t before = (uint64_t)keys * (unsigned)split;
+    const unsigned left = before < span ? span - (unsigned)before : 0;
+    const unsigned mine = left < keys ? left : keys;
+    const unsigned from = (unsigned)r.hi - left;
+    return {from, from + mine};
+}
+
+// The step after t0 < to, or t0 again if that is the last one.
+__host__ __device__ __forceinline__ unsigned step_after(unsigned t0, unsigned to, unsigned step)
+{
+    return to - t0 > step ? t0 + step : t0;
 }
 
 }  // namespace qmm

@@ -91,11 +91,48 @@ void visible_keys()
                 }
 }
 
+// Parts and steps cover a tile's keys once, in order, at every length; the places
+// that a step looks up lie before the part's end. The last steps of long parts
+// stand for the others.
+void parts_and_steps()
+{
+    const int most = INT_MAX - 15;
+    for (int hi : {0, 1, 31, 32, 33, 257, 5000, 1 << 30, most - 256, most - 1, most})
+        for (int lo : {0, 5, 64, hi - 1000, hi - 300, hi - 32, hi - 1, hi, hi + 7})
+            for (int splits : {1, 2, 17, 2048})
+                for (int min_part : {1, 256, 2048, INT_MAX})
+                    for (int waves : {4, 8}) {
+                        if (lo < 0 || lo > most) continue;
+                        const unsigned step = (unsigned)waves * qmm::kKeys;
+                        const unsigned start = (unsigned)lo / 32 * 32;
+                        const qmm::Reach reach = {lo, hi, lo, hi};
+                        unsigned end = start < (unsigned)hi ? start : (unsigned)hi;
+                        for (int split = 0; split < splits; ++split) {
+                            const auto [from, to] = qmm::part_of(reach, split, splits, min_part, (int)step);
+                            CHECK(from == end && to >= from && to <= (unsigned)hi);
+                            CHECK(from == to || from % 32 == 0);
+                            end = to;
+                            for (unsigned wave = 0; wave < (unsigned)waves; ++wave) {
+                                unsigned t0 = from + wave * qmm::kKeys;
+                                if (t0 < to && to - t0 > 4 * step) t0 += (to - t0) / step * step - 2 * step;
+                                for (int n = 0; t0 < to; t0 += step, ++n) {
+                                    CHECK(n < 4 && t0 + qmm::kKeys - 1 <= (unsigned)INT_MAX);
+                                    const unsigned next = qmm::step_after(t0, to, step);
+                                    CHECK(next < to && (next == t0 + step || (next == t0 && t0 + step >= to)));
+                                    CHECK(qmm::kv_entry((int)next + 16, 4, most / 16 - 1) < most / 16);
+                                }
+                            }
+                        }
+                        CHECK(end == (unsigned)hi);
+                    }
+}
+
 }  // namespace
 
 int main()
 {
     fitting();
+    parts_and_steps();
     visible_keys();
     groups();
     ring_places();
