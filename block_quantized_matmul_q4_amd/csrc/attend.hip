@@ -54,6 +54,7 @@
 // it by 2 and compared through them (96 -> 89 us), scales shared by DPP
 // broadcasts, accumulators in ordinary registers.
 #include "qmm_attend.h"
+#include "qmm_attend_shape.h"
 
 namespace qmm {
 namespace {
@@ -83,11 +84,11 @@ __global__ void __launch_bounds__(WAVES * 64, (kWavesPerSimd<NB, PACK, WAVES>)) 
 
     const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int units = a.batch * a.cache.kv_heads;
+    const int units = a.requests * a.cache.kv_heads;
     const int unit = unit_of(blockIdx.x, units);
     const int split = blockIdx.x / units % a.splits;
     const int tile0 = blockIdx.x / units / a.splits;
-    const int b = unit / a.cache.kv_heads, kvh = unit % a.cache.kv_heads;
+    const int b = a.first + unit / a.cache.kv_heads, kvh = unit % a.cache.kv_heads;
     const int shift = __builtin_ctz(a.cache.page_size);
     const KvRequest request = kv_request(a.cu, a.lens, b, a.tokens, a.width, shift);
     const int q0 = request.q0;
@@ -349,11 +350,11 @@ __global__ void __launch_bounds__(WAVES * 64, (kWavesPerSimd<NB, PACK, WAVES>)) 
 // A few parts: D / 4 threads per row, each for itself.
 constexpr int kFewSplits = 16;
 
-__global__ void __launch_bounds__(256) join_few_kernel(AttendArgs a)
+__global__ void __launch_bounds__(256) join_few_kernel(AttendArgs a, int64_t first)
 {
     const int D = a.cache.head_dim, wide = D / 4;
     const int64_t rows_all = (int64_t)a.tokens * a.q_heads;
-    const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x, row = id / wide;
+    const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x, row = first + id / wide;
     if (row >= rows_all || row / a.q_heads >= a.cu[a.batch]) return;
     const int c = (int)(id % wide) * 4;
     const float2 *ml = (const float2 *)a.part_ml + row;
@@ -395,16 +396,15 @@ __global__ void __launch_bounds__(256) join_few_kernel(AttendArgs a)
 // Joins the parts of each row: out = sum_i 2^(m_i - m) o_i / sum_i 2^(m_i - m) l_i.
 // One workgroup per row: the parts' weights first, then groups of D / 4 threads
 // share the parts out, so that many parts are many loads in flight.
-constexpr int kMaxSplits = 2048;
 constexpr int kJoinThreads = 512;
 
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(AttendArgs a)
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(AttendArgs a, int64_t first)
 {
     __shared__ float s_w[kMaxSplits], s_wave[kJoinThreads / 64];
     __shared__ float s_l[kMaxSplits];
     __shared__ f32x4 s_o[kJoinThreads];
     const int D = a.cache.head_dim, tid = threadIdx.x, wave = tid >> 6;
-    const int64_t rows_all = (int64_t)a.tokens * a.q_heads, row = blockIdx.x;
+    const int64_t rows_all = (int64_t)a.tokens * a.q_heads, row = first + blockIdx.x;
     if (row / a.q_heads >= a.cu[a.batch]) return;
     float m = kNone;
     for (int s = tid; s < a.splits; s += kJoinThreads) {
@@ -451,48 +451,10 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttendArgs a)
 
 }  // namespace
 
-// Workgroups of four waves that the chip holds at once, two waves per SIMD.
-constexpr int64_t kResident = 512;
-
 AttendShape attend_shape(int tokens, int batch, int kv_heads, int group, int head_dim,
                          int64_t max_q, int64_t max_len, int64_t window)
 {
-    if (max_q > tokens) max_q = tokens > 0 ? tokens : 1;
-    if (window > 0 && max_len > window + max_q) max_len = window + max_q;
-    const int64_t packed = max_q * group;
-    // Two tiles of 16 rows share each decoded key where their registers leave room
-    // for two waves per SIMD, and where there is work for every workgroup slot (a
-    // prompt of 2048, 32/8 heads of 128: 147 -> 133 us; of 512, 16 heads of 64, which
-    // has less: 8.9 -> 15.5 us; 8/2 heads of 256, one wave per SIMD: 79 -> 91 us).
-    const bool few = packed <= 16;
-    const bool twice = head_dim <= 128 && (int64_t)batch * kv_heads * ((packed + 31) / 32) >= kResident;
-    const int rows = packed <= 8 ? 8 : twice && !few ? 32 : 16;
-    const int64_t tiles = (packed + rows - 1) / rows;
-    const int64_t units = (int64_t)batch * kv_heads * tiles;
-    // Keys of a part: few enough that every workgroup slot has one, and, once
-    // there is enough work, so few that ragged requests even out (four parts
-    // to a slot), but no less than what pays for joining them
-    const int64_t all = units * max_len;
-    int64_t part;
-    if (!few) {
-        part = all / (16 * kResident);
-        // (300 rows over 3000 keys, 32/8 heads of 128, parts of 2048 -> of one per
-        // slot: 89 -> 81 us)
-        const int64_t each = all / kResident;
-        if (part < 2048) part = each < 256 ? 256 : each < 2048 ? each : 2048;
-    } else if (units <= kResident / 2 && max_len * head_dim <= 512 * 256) {
-        // short requests: eight waves and one launch (16 requests' 4 rows over
-        // 1028 keys, 16 heads of 64: 15.4 -> 10.8 us; one over 470, 8/2 heads of
-        // 256: 12.8 -> 13.7 us on the GPU, and a launch less to pay for)
-        return {(int)tiles, 1, (int)max_len, rows, 8, few};
-    } else {
-        part = all / (4 * kResident);
-        if (part < 1024) part = all / kResident < 1024 ? all / kResident : 1024;
-        if (part < 256) part = 256;
-    }
-    int64_t splits = (max_len + part - 1) / part;
-    if (splits > kMaxSplits) splits = kMaxSplits;
-    return {(int)tiles, (int)splits, (int)(part < INT32_MAX ? part : INT32_MAX), rows, 4, few};
+    return attend_shape_of(tokens, batch, kv_heads, group, head_dim, max_q, max_len, window);
 }
 
 template <int NB, bool PACK>
@@ -513,28 +475,41 @@ static void launch_few(const AttendArgs &a, unsigned grid, hipStream_t stream)
         launch_few<NB, false>(a, grid, stream);
 }
 
-hipError_t launch_attend(const AttendArgs &a, hipStream_t stream)
+static hipError_t launch_requests(const AttendArgs &a, hipStream_t stream)
 {
-    const int64_t grid = (int64_t)a.batch * a.cache.kv_heads * a.tiles * a.splits;
-    if (grid > INT32_MAX) return hipErrorInvalidConfiguration;
+    const unsigned grid = (unsigned)a.requests * a.cache.kv_heads * a.tiles * a.splits;
     if (!a.few) {
-        launch_attend_many(a, (unsigned)grid, stream);
+        launch_attend_many(a, grid, stream);
     } else {
         switch (a.cache.head_dim) {
-        case 64: launch_few<2>(a, (unsigned)grid, stream); break;
-        case 96: launch_few<3>(a, (unsigned)grid, stream); break;
-        case 128: launch_few<4>(a, (unsigned)grid, stream); break;
-        case 192: launch_few<6>(a, (unsigned)grid, stream); break;
-        case 256: launch_few<8>(a, (unsigned)grid, stream); break;
+        case 64: launch_few<2>(a, grid, stream); break;
+        case 96: launch_few<3>(a, grid, stream); break;
+        case 128: launch_few<4>(a, grid, stream); break;
+        case 192: launch_few<6>(a, grid, stream); break;
+        case 256: launch_few<8>(a, grid, stream); break;
         default: return hipErrorInvalidValue;
         }
     }
-    if (hipError_t err = hipGetLastError()) return err;
-    if (a.splits > 1 && a.splits <= kFewSplits) {
-        const int64_t threads = (int64_t)a.tokens * a.q_heads * (a.cache.head_dim / 4);
-        join_few_kernel<<<(unsigned)((threads + 255) / 256), 256, 0, stream>>>(a);
-    } else if (a.splits > 1) {
-        join_kernel<<<(unsigned)(a.tokens * a.q_heads), kJoinThreads, 0, stream>>>(a);
+    return hipGetLastError();
+}
+
+hipError_t launch_attend(const AttendArgs &args, hipStream_t stream)
+{
+    AttendArgs a = args;
+    const int most = requests_per_launch(a.cache.kv_heads, a.tiles, a.splits);
+    for (a.first = 0; a.first < a.batch; a.first += a.requests) {
+        a.requests = a.batch - a.first < most ? a.batch - a.first : most;
+        if (hipError_t err = launch_requests(a, stream)) return err;
+    }
+    const int64_t rows = (int64_t)a.tokens * a.q_heads;
+    for (int64_t first = 0; a.splits > 1 && first < rows; first += kJoinRows) {
+        const int64_t n = rows - first < kJoinRows ? rows - first : kJoinRows;
+        if (a.splits <= kFewSplits) {
+            const int64_t threads = n * (a.cache.head_dim / 4);
+            join_few_kernel<<<(unsigned)((threads + 255) / 256), 256, 0, stream>>>(a, first);
+        } else {
+            join_kernel<<<(unsigned)n, kJoinThreads, 0, stream>>>(a, first);
+        }
     }
     return hipGetLastError();
 }

@@ -63,11 +63,11 @@ __global__ void __launch_bounds__(kWaves * 64, 2) attend_many_kernel(AttendArgs 
 
     const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int units = a.batch * a.cache.kv_heads;
+    const int units = a.requests * a.cache.kv_heads;
     const int unit = unit_of(blockIdx.x, units);
     const int split = blockIdx.x / units % a.splits;
     const int tile0 = a.tiles - 1 - (int)(blockIdx.x / units / a.splits);
-    const int b = unit / a.cache.kv_heads, kvh = unit % a.cache.kv_heads;
+    const int b = a.first + unit / a.cache.kv_heads, kvh = unit % a.cache.kv_heads;
     const int shift = __builtin_ctz(a.cache.page_size);
     const KvRequest request = kv_request(a.cu, a.lens, b, a.tokens, a.width, shift);
     const int q0 = request.q0;

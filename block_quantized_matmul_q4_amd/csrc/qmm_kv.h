@@ -112,6 +112,7 @@ struct AttendArgs {
     float *part_o;          // [splits][tokens * q_heads][head_dim], splits > 1
     float *part_ml;         // [splits][tokens * q_heads][2]
     int tokens, batch, q_heads, group;
+    int first, requests;    // those of this launch
     int tiles;              // row tiles per (request, KV head) in the grid
     int tile_rows;          // rows of such a tile
     int splits;             // parts of a request's keys

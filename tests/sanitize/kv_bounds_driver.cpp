@@ -1,7 +1,9 @@
 // Runs the index arithmetic that the kernels of the paged KV cache share
-// (csrc/qmm_kv.h, csrc/qmm_attend_rows.h) on the host, built with AddressSanitizer and
+// (csrc/qmm_kv.h, csrc/qmm_attend_rows.h) and the rules by which attention is
+// launched (csrc/qmm_attend_shape.h) on the host, built with AddressSanitizer and
 // UndefinedBehaviorSanitizer, over sums and lengths next to and past the ends of
-// 32 bits. Exits non-zero on the first failed check.
+// 32 bits. Exits non-zero on the first failed check. With the eight sizes of a
+// call as arguments it prints that call's launch instead.
 #include <climits>
 #include <cstdint>
 #include <cstdio>
@@ -9,6 +11,7 @@
 #include <vector>
 
 #include "../../block_quantized_matmul_q4_amd/csrc/qmm_attend_rows.h"
+#include "../../block_quantized_matmul_q4_amd/csrc/qmm_attend_shape.h"
 #include "../../block_quantized_matmul_q4_amd/csrc/qmm_kv.h"
 
 namespace {
@@ -127,10 +130,47 @@ void parts_and_steps()
                     }
 }
 
+// Every launch of every accepted size holds less than 2^32 threads, and the launches
+// of a call have each request once.
+void launches()
+{
+    for (int batch : {1, 7, 512, 513, 1 << 16, 600000, 1 << 20})
+        for (int kv_heads : {1, 8, 1024})
+            for (int group : {1, 8, 64})
+                for (int64_t tokens : {(int64_t)1, (int64_t)16384, (int64_t)INT_MAX / (kv_heads * group)})
+                    for (int64_t max_q : {(int64_t)1, (int64_t)33, (int64_t)16384, (int64_t)INT_MAX / 64})
+                        for (int64_t max_len : {(int64_t)1, (int64_t)5000, (int64_t)1 << 20, (int64_t)INT_MAX})
+                            for (int64_t window : {(int64_t)0, (int64_t)4096, (int64_t)INT_MAX})
+                                for (int dim : {64, 256}) {
+                                    const auto s = qmm::attend_shape_of((int)tokens, batch, kv_heads, group, dim,
+                                                                        max_q, max_len, window);
+                                    CHECK(s.tiles >= 1 && s.splits >= 1 && s.splits <= qmm::kMaxSplits);
+                                    CHECK(s.min_part >= 1 && (s.waves == 4 || s.waves == 8));
+                                    const int most = qmm::requests_per_launch(kv_heads, s.tiles, s.splits);
+                                    const int64_t n = most < batch ? most : batch;
+                                    CHECK(n >= 1 && n * kv_heads * s.tiles * s.splits * s.waves * 64 < (int64_t)1 << 32);
+                                    const int64_t rows = tokens * kv_heads * group;
+                                    const int64_t joined = rows < qmm::kJoinRows ? rows : qmm::kJoinRows;
+                                    CHECK(joined * 512 < (int64_t)1 << 32);
+                                    // rows that one workgroup would walk on to although the chip is not full
+                                    const int64_t groups = (int64_t)batch * kv_heads * s.tiles;
+                                    const int64_t packed = (max_q < tokens ? max_q : tokens) * group;
+                                    CHECK((int64_t)s.tiles * s.tile_rows >= packed || groups > qmm::kLaunchTiles / 2);
+                                }
+}
+
 }  // namespace
 
-int main()
+int main(int argc, char **argv)
 {
+    if (argc == 9) {
+        int64_t v[8];
+        for (int i = 0; i < 8; ++i) v[i] = std::atoll(argv[i + 1]);
+        const auto s = qmm::attend_shape_of((int)v[0], (int)v[1], (int)v[2], (int)v[3], (int)v[4], v[5], v[6], v[7]);
+        std::printf("%d %d %d %d %d %d\n", s.tiles, s.splits, s.min_part, s.tile_rows, s.waves, (int)s.few);
+        return 0;
+    }
+    launches();
     fitting();
     parts_and_steps();
     visible_keys();

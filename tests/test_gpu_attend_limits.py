@@ -1,6 +1,8 @@
 """Attention at the ends of what its arguments may be: windows, lengths and launches next to
 the ends of 32 bits. Tolerances are those of test_gpu_kv.py."""
 
+import copy
+
 import numpy as np
 import pytest
 import torch
@@ -59,3 +61,54 @@ def test_all_tokens_of_the_longest_request(new):
     want = lse + np.log(2.0**27 - 1)
     assert (np.abs(got_lse - want) <= e + 2.0**-8 + 1e-6 * (1 + np.abs(want))).all()
     assert (np.abs(got - o) <= (2 * e[..., None] + 2.0**-6 + 2.0**-8) * size + 2.0**-29).all()
+
+
+def same_as_reference(s, b, o, lse, **args):
+    """Checks request b's rows of a batch whose results are o, lse."""
+    one, rows = copy.copy(s), slice(int(s.cu[b]), int(s.cu[b + 1]))
+    one.q, one.table, one.lens = s.q[rows], s.table[b:b + 1], s.lens[b:b + 1]
+    one.cu = s.cu[b:b + 2] - s.cu[b]
+    one.run = lambda **_: (o[rows].cpu().numpy().astype(np.float64), lse[rows].cpu().numpy().astype(np.float64))
+    one.check(**args)
+
+
+def test_default_hints_of_a_large_batch():
+    """512 requests of 32 rows, each of them launched for all 16384: as many tiles as 2^32 threads."""
+    rng = np.random.default_rng(5)
+    s = Setup([int(n) for n in rng.integers(20, 120, 512)], [32] * 512, 8, 8, 64, 16)
+    args = [gpu(x) for x in (s.q, s.cache, s.table, s.lens, s.cu)]
+    o, lse = qmm.attend_q4_0(*args, return_lse=True)
+    want = qmm.attend_q4_0(*args, max_q=32, return_lse=True)
+    assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+    for b in (0, 300, 511):
+        same_as_reference(s, b, o, lse)
+
+
+@pytest.mark.parametrize("news,group", [([2, 1, 2, 1, 1, 2], 1), ([20, 3, 19, 1, 0, 20], 2)])
+def test_more_requests_than_one_launch_takes(news, group):
+    """600000 requests of 8 heads; those with rows are at the ends of the launches."""
+    batch, at = 600000, [0, 262143, 262144, 524287, 524288, 599999]
+    s = Setup([100, 37, 64, 5, 20, 111], news, 8, group, 64, 16)
+    table = torch.zeros(batch, s.table.shape[1], dtype=torch.int32, device="cuda")
+    lens, rows = (torch.zeros(batch, dtype=torch.int32, device="cuda") for _ in range(2))
+    table[at], lens[at] = gpu(s.table), gpu(s.lens)
+    rows[at] = torch.tensor(news, dtype=torch.int32, device="cuda")
+    cu = torch.cat([rows.new_zeros(1), rows.cumsum(0).int()])
+    s.run = lambda **args: [x.cpu().numpy().astype(np.float64) for x in qmm.attend_q4_0(
+        gpu(s.q), gpu(s.cache), table, lens, cu, max_q=max(news), return_lse=True, **args)]
+    s.check()
+
+
+@pytest.mark.parametrize("max_q", [1, 3])               # more than 16 parts, and fewer
+def test_more_rows_than_one_join_takes(max_q):
+    """16395 rows of 64 heads in 15 and 20 parts; all but five belong to a request without tokens."""
+    s = Setup([5000, 5000], [2, 3], 1, 64, 64, 16)
+    q = torch.randn(16395, 64, 64, device="cuda")
+    q[:2], q[-3:] = gpu(s.q[:2]), gpu(s.q[2:])
+    table, lens = gpu(s.table[[0, 0, 1]]), torch.tensor([5000, 0, 5000], dtype=torch.int32, device="cuda")
+    cu = torch.tensor([0, 2, 16392, 16395], dtype=torch.int32, device="cuda")
+    out, lse = torch.full_like(q, 7.0), torch.full((16395, 64), 7.0, device="cuda")
+    qmm.attend_q4_0(q, gpu(s.cache), table, lens, cu, max_q=max_q, out=out, lse=lse)
+    assert not out[2:-3].any() and (lse[2:-3] == -np.inf).all()
+    s.run = lambda **_: [torch.cat([x[:2], x[-3:]]).cpu().numpy().astype(np.float64) for x in (out, lse)]
+    s.check()

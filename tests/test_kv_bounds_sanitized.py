@@ -1,6 +1,7 @@
 """The index arithmetic of the paged KV cache's kernels (csrc/qmm_kv.h and
-csrc/qmm_attend_rows.h) next to and past the ends of 32 bits, built for the host
-with AddressSanitizer and UndefinedBehaviorSanitizer and run by
+csrc/qmm_attend_rows.h) and the rules of attention's launches
+(csrc/qmm_attend_shape.h), next to and past the ends of 32 bits, built for the
+host with AddressSanitizer and UndefinedBehaviorSanitizer and run by
 tests/sanitize/kv_bounds_driver.cpp. CPU only."""
 
 import os
