@@ -347,6 +347,14 @@ __global__ void __launch_bounds__(WAVES * 64, (kWavesPerSimd<NB, PACK, WAVES>)) 
     }
 }
 
+// Rows before cu[0] and from cu[B] on belong to no request: no part of them is
+// written, and they are not either.
+__device__ __forceinline__ bool of_a_request(const AttendArgs &a, int64_t row)
+{
+    const int64_t token = row / a.q_heads;
+    return token >= a.cu[0] && token < a.cu[a.batch];
+}
+
 // A few parts: D / 4 threads per row, each for itself.
 constexpr int kFewSplits = 16;
 
@@ -355,7 +363,7 @@ __global__ void __launch_bounds__(256) join_few_kernel(AttendArgs a, int64_t fir
     const int D = a.cache.head_dim, wide = D / 4;
     const int64_t rows_all = (int64_t)a.tokens * a.q_heads;
     const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x, row = first + id / wide;
-    if (row >= rows_all || row / a.q_heads >= a.cu[a.batch]) return;
+    if (row >= rows_all || !of_a_request(a, row)) return;
     const int c = (int)(id % wide) * 4;
     const float2 *ml = (const float2 *)a.part_ml + row;
     float m = kNone;
@@ -405,7 +413,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttendArgs a, int64_
     __shared__ f32x4 s_o[kJoinThreads];
     const int D = a.cache.head_dim, tid = threadIdx.x, wave = tid >> 6;
     const int64_t rows_all = (int64_t)a.tokens * a.q_heads, row = first + blockIdx.x;
-    if (row / a.q_heads >= a.cu[a.batch]) return;
+    if (!of_a_request(a, row)) return;
     float m = kNone;
     for (int s = tid; s < a.splits; s += kJoinThreads) {
         const float *ml = a.part_ml + (s * rows_all + row) * 2;

@@ -34,3 +34,20 @@ def test_visible_nan_far_below_the_maximum(keys, new):
     o, lse = s.check(max_q=new)
     assert np.isnan(o[..., 32:]).all() and np.isfinite(o[..., :32]).all() and np.isfinite(lse).all()
     assert (lse > others + 350).all()
+
+
+@pytest.mark.parametrize("keys", PARTS)
+@pytest.mark.parametrize("new", [2, 40])
+def test_rows_of_no_request_are_left(keys, new):
+    """Before cu[0] and from cu[B] on, whatever the workspace held."""
+    s = Setup([keys, 30], [new, 3], 1, 2, 64, 16)
+    n = new + 3
+    q = torch.randn(n + 7, 2, 64, device="cuda")
+    q[4:n + 4] = gpu(s.q)
+    out, lse = torch.full_like(q, 7.0), torch.full((n + 7, 2), 7.0, device="cuda")
+    qmm.attend_q4_0(q, gpu(s.cache), gpu(s.table), gpu(s.lens), gpu(s.cu + 4), out=out, lse=lse, max_q=new,
+                    workspace=torch.full((1 << 24,), 63, dtype=torch.uint8, device="cuda"))
+    for x in (out, lse):
+        assert (x[:4] == 7).all() and (x[n + 4:] == 7).all()
+    s.run = lambda **_: [x[4:n + 4].cpu().numpy().astype(np.float64) for x in (out, lse)]
+    s.check()
