@@ -520,7 +520,7 @@ def attend_q4_0(q, cache, table, lens, cu, *, scale=None, causal: bool = True, w
     pages, kv_heads, _ = sizes
     page_size = geometry.page_size
     batch, width = _sizes("table", table, int32, 2, index)
-    if heads == 0 or heads % kv_heads:
+    if heads == 0 or kv_heads == 0 or heads % kv_heads:
         raise ValueError(f"q has {heads} heads, not a multiple of the cache's {kv_heads}")
     if out is None:
         out = q.new_empty((tokens, heads, dim))

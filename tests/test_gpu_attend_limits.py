@@ -112,3 +112,12 @@ def test_more_rows_than_one_join_takes(max_q):
     assert not out[2:-3].any() and (lse[2:-3] == -np.inf).all()
     s.run = lambda **_: [torch.cat([x[:2], x[-3:]]).cpu().numpy().astype(np.float64) for x in (out, lse)]
     s.check()
+
+
+def test_a_cache_without_heads_or_pages_is_refused():
+    s = Setup([10], [1], 1, 1, 64, 16)
+    rest = [gpu(x) for x in (s.table, s.lens, s.cu)]
+    for pages, heads in ((3, 0), (0, 1), (0, 0)):
+        cache = torch.empty(pages, heads, 1152, dtype=torch.uint8, device="cuda")
+        with pytest.raises((ValueError, qmm.QmmError), match="multiple|num_pages"):
+            qmm.attend_q4_0(gpu(s.q), cache, *rest)
