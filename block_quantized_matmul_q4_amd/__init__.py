@@ -23,7 +23,7 @@ The paged Q4_0 KV cache has both layers too: ``qmm_kv_plan``,
 
     step = kv_plan(want, lens, table, ring, pool, tokens, page_size)
     kv_append_q4_0(k, v, cache, step.slots)
-    out = attend_q4_0(q, cache, table, step.lens, step.cu)
+    out = attend_q4_0(q, cache, table, step.lens, step.cu, max_q=1)     # decoding
 
 There is no fallback: if ``libqmm.so`` is missing, every call raises.
 Build it with ``python -m block_quantized_matmul_q4_amd._build``.
@@ -410,7 +410,9 @@ def kv_plan(want, lens, table, ring, pool, tokens: int, page_size: int, out=None
     want, lens int32 [B]; table int32 [B, width] and ring int32 [ring size] are
     updated in place; pool int64 [2] holds (head, count) of the ring. Returns a
     KvPlan of new tensors, or fills and returns ``out``, whose lens and pool
-    may be the inputs themselves and whose positions may be None.
+    may be the inputs themselves and whose positions may be None. A request
+    that is refused (status KV_NO_PAGES or KV_NO_ROWS) keeps its rows in cu, with
+    slots of -1: what attention then writes to them means nothing.
     """
     import torch
 
@@ -505,8 +507,9 @@ def attend_q4_0(q, cache, table, lens, cu, *, scale=None, causal: bool = True, w
     Rows cu[b] .. cu[b + 1] - 1 are the last tokens of request b, which has
     lens[b] tokens in the pages table[b]. scale defaults to head_dim ** -0.5;
     max_q and max_len are the largest number of rows and of tokens expected of
-    a request (all rows and the table's width if not given; decoding callers
-    should say max_q=1). workspace: a uint8 tensor to use instead of a new one.
+    a request (all rows and the table's width if not given, which is right but
+    launched as one long prompt: decoding callers should say max_q=1). Rows
+    before cu[0] and from cu[-1] on are left as they are. workspace: a uint8 tensor to use instead of a new one.
     Returns out float32 [T, q_heads, head_dim], with return_lse also lse
     float32 [T, q_heads].
     """

@@ -45,10 +45,15 @@
 // table's entries a step further ahead, the waves of a workgroup share a part of
 // the keys and join through LDS, and long requests are split over workgroups
 // whose parts a second launch joins.
-// Measured, 32/8 heads of 128: 64 requests up to 8192 keys (335 MB of codes) 89
-// us, 3.8 TB/s, and 5 us for the join; one of 131072 keys 35 + 7 us. 8/2 heads of
-// 256, 32 requests up to 2351 keys 18 + 4 us, two thirds of it the time from the
-// launch to the first scores. Steps that paid: the table read through the
+// Measured, 32/8 heads of 128: 64 requests up to 8192 keys (335 MB of codes) 88
+// us, 3.8 TB/s, and 5 us for the join; one of 131072 keys 36 + 7 us. 8/2 heads of
+// 256, 32 requests up to 2351 keys 18 + 4 us. What a call takes apart from its keys
+// (in a graph, where an empty kernel takes 2.4 us), at 256 dims: 8.8 us for 576
+// workgroups of four waves, 15.3 with one step of 128 keys, 4.5 us for each further
+// one; 6.0 us for 32 of eight waves, 10.2 with one step of 256 keys, 3.0 us for each
+// further one. At 64 dims 4.6, 6.8 and 1.4 us; 4.0, 5.6 and 1.0 us. With tiles of 16
+// rows at 256 dims 24 registers are spilled, some of them in the key loop; all other
+// forms spill no vector register. Steps that paid: the table read through the
 // constant address space and a step ahead (a vector load waits for all loads in
 // flight, 109 -> 96 us), the running maximum moved only when the exponents pass
 // it by 2 and compared through them (96 -> 89 us), scales shared by DPP

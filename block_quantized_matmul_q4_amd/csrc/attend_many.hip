@@ -27,13 +27,14 @@
 // instructions of 16 cycles and 520 other operations of 4), two waves per SIMD.
 // Up to 128 dims QT = 2 where there is work for every workgroup slot; wider rows
 // take QT = 1, since two tiles' registers leave one wave per SIMD (a prompt of
-// 2048 tokens, 8/2 heads of 256: 87 us, with QT = 1 78 us). Four chunks of up
-// to 512 tokens over 5000 to 16384 keys, 32/8 heads of 128, 919 us (0.31 PFLOP/s; the
-// matrix cores are busy 32 % of the time) and 21 us for the join. Decoding once per
-// 128 rows into LDS, a barrier every 32 keys, was built: half of the vector
-// operations, at 128 dims the same time, at 192 and 256 dims 8 to 10 % less for
-// 512 rows and more over 16384 keys and twice the time for 512 tokens; it is not
-// kept.
+// 2048 tokens, 8/2 heads of 256: 87 us, with QT = 1 78 us, both with a kernel trace
+// attached; a whole call takes 68 us without). Four chunks of up to 512 tokens over
+// 5000 to 16384 keys, 32/8 heads of 128, 901 us (0.32 PFLOP/s; the matrix cores are
+// busy 32 % of the time and the vector ALU 59 %, one after the other) and 20 us for
+// the join. Decoding once per 128 rows into LDS, a barrier every 32 keys, was built:
+// half of the vector operations, at 128 dims the same time, twice the time for 512
+// tokens, and for four chunks of 512 over 16384 keys, 8/2 heads of 256, 787 us where
+// this kernel takes 837; it is not kept.
 #include "qmm_attend.h"
 
 namespace qmm {

@@ -23,7 +23,10 @@ inline int requests_per_launch(int kv_heads, int tiles, int splits)
     return most > 1 ? (int)most : 1;
 }
 
-// Workgroups of four waves that the chip holds at once, two waves per SIMD.
+// Workgroups of four waves that the chip holds at once with two waves per SIMD, as
+// the kernels for many rows have. Those for 8 rows have room for three up to 128
+// dims and for four at 64, which no rule here uses: 131072 keys of 32/8 heads
+// of 128 make 1024 workgroups, where 768 run at once.
 constexpr int64_t kResident = 512;
 
 inline AttendShape attend_shape_of(int tokens, int batch, int kv_heads, int group, int head_dim,
@@ -35,7 +38,15 @@ inline AttendShape attend_shape_of(int tokens, int batch, int kv_heads, int grou
     // Two tiles of 16 rows share each decoded key where their registers leave room
     // for two waves per SIMD, and where there is work for every workgroup slot (a
     // prompt of 2048, 32/8 heads of 128: 147 -> 133 us; of 512, 16 heads of 64, which
-    // has less: 8.9 -> 15.5 us; 8/2 heads of 256, one wave per SIMD: 79 -> 91 us).
+    // has less: 8.9 -> 15.5 us; 8/2 heads of 256, one wave per SIMD: 79 -> 91 us; all
+    // with a kernel trace attached, without which these calls take 113, 8.5 and 68 us).
+    //
+    // 9 to 16 rows by the kernel for few rows -> by the other one, whole calls in a
+    // graph, 4 rows x group 4: where requests fill the chip, up to 128 dims, it is the
+    // faster (64 requests of 4000 keys, 8 KV heads of 64: 49 -> 67 us, of 128: 91 -> 117
+    // us); 16 requests of 2000 20.5 -> 20.2, of 8000 46.9 -> 44.4 us at 128 dims. At 256
+    // dims its tiles of 16 rows spill 24 registers and lose throughout (16 requests of
+    // 8000 keys, 2 KV heads: 37.7 -> 30.8 us).
     const bool few = packed <= 16;
     const bool twice = head_dim <= 128 && (int64_t)batch * kv_heads * ((packed + 31) / 32) >= kResident;
     const int rows = packed <= 8 ? 8 : twice && !few ? 32 : 16;
@@ -57,9 +68,11 @@ inline AttendShape attend_shape_of(int tokens, int batch, int kv_heads, int grou
         const int64_t each = all / kResident;
         if (part < 2048) part = each < 256 ? 256 : each < 2048 ? each : 2048;
     } else if (units <= kResident / 2 && max_len * head_dim <= 512 * 256) {
-        // short requests: eight waves and one launch (16 requests' 4 rows over
-        // 1028 keys, 16 heads of 64: 15.4 -> 10.8 us; one over 470, 8/2 heads of
-        // 256: 12.8 -> 13.7 us on the GPU, and a launch less to pay for)
+        // Short requests: eight waves and one launch, a launch less for the host (3 to 4
+        // us a call outside of graphs). Parts of four waves and a join -> this, in a
+        // graph: 32 requests of 1024 keys, 32/8 heads of 64, 12.9 -> 10.0 us, of 512 at
+        // 128 dims 12.8 -> 9.8 us; but one of 512 at 256 dims 12.6 -> 13.5 us, one of
+        // 1024 at 128 dims 9.8 -> 12.3 us, and one of 2048 at 64 dims 8.6 -> 13.7 us.
         return {(int)tiles, 1, (int)max_len, rows, 8, few};
     } else {
         part = all / (4 * kResident);

@@ -8,7 +8,7 @@ its cache:
     step = kv_plan(want, lens, table, ring, pool, tokens, page_size)
     q, k, v = x @ Wq, x @ Wk, x @ Wv
     kv_append_q4_0(k, v, cache, step.slots)
-    y = attend_q4_0(q, cache, table, step.lens, step.cu) @ Wo
+    y = attend_q4_0(q, cache, table, step.lens, step.cu, max_q=1) @ Wo     # decoding
 
 Each step's attention is compared with plain attention in 64 bits over the
 values that the cache holds (kv_read_q4_0). Requests end on the way and give

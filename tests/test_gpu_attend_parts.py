@@ -51,3 +51,17 @@ def test_rows_of_no_request_are_left(keys, new):
         assert (x[:4] == 7).all() and (x[n + 4:] == 7).all()
     s.run = lambda **_: [x[4:n + 4].cpu().numpy().astype(np.float64) for x in (out, lse)]
     s.check()
+
+
+@pytest.mark.parametrize("dim,keys", [(128, 700), (64, 6000)])
+def test_a_batch_in_two_calls(dim, keys):
+    """Decoding requests first, prompt chunks after them: each call writes its requests' rows of the
+    same out, by slices of the table, the lengths and cu."""
+    s = Setup([keys, 300, 40, 400, 90], [1, 1, 1, 50, 33], 2, 4, dim, 16)
+    q, cache, table, lens, cu = (gpu(x) for x in (s.q, s.cache, s.table, s.lens, s.cu))
+    out, lse = torch.full_like(q, 7.0), torch.full(q.shape[:2], 7.0, device="cuda")
+    qmm.attend_q4_0(q, cache, table[:3], lens[:3], cu[:4], max_q=1, out=out, lse=lse)
+    assert (out[3:] == 7).all() and (lse[3:] == 7).all()
+    qmm.attend_q4_0(q, cache, table[3:], lens[3:], cu[3:], max_q=50, out=out, lse=lse)
+    s.run = lambda **_: [x.cpu().numpy().astype(np.float64) for x in (out, lse)]
+    s.check()
