@@ -156,26 +156,28 @@ QMM_API int qmm_kv_plan(const int32_t *want, const int32_t *lens, int32_t *table
     for (const void *p : {(const void *)pool, (const void *)new_pool, (const void *)slots})
         if (misaligned(p, 8))
             return fail(QMM_EALIGN, "%s: misaligned pointer (int64 arrays need 8 bytes)", fn);
-    const struct { const void *p; uint64_t n; bool out; } parts[] = {
-        {want, 4u * (uint64_t)B, false},
-        {lens, 4u * (uint64_t)B, false},
-        {pool, 16, false},
-        {table, 4u * (uint64_t)B * (uint64_t)width, true},
-        {ring, 4u * (uint64_t)ring_size, true},
-        {new_lens, 4u * (uint64_t)B, true},
-        {new_pool, 16, true},
-        {cu, 4u * ((uint64_t)B + 1), true},
-        {slots, 8u * (uint64_t)T, true},
-        {positions, positions ? 4u * (uint64_t)T : 0, true},
-        {status, 4u * (uint64_t)B, true},
+    enum { kWant, kLens, kPool, kTable, kRing, kNewLens, kNewPool, kCu, kSlots, kPositions, kStatus };
+    const struct { const void *p; uint64_t n; } parts[] = {
+        {want, 4u * (uint64_t)B},
+        {lens, 4u * (uint64_t)B},
+        {pool, 16},
+        {table, 4u * (uint64_t)B * (uint64_t)width},
+        {ring, 4u * (uint64_t)ring_size},
+        {new_lens, 4u * (uint64_t)B},
+        {new_pool, 16},
+        {cu, 4u * ((uint64_t)B + 1)},
+        {slots, 8u * (uint64_t)T},
+        {positions, positions ? 4u * (uint64_t)T : 0},
+        {status, 4u * (uint64_t)B},
     };
-    for (const auto &x : parts)
-        for (const auto &y : parts) {
-            if (&x >= &y || !(x.out || y.out) || !x.n || !y.n) continue;
-            if ((x.p == lens && y.p == new_lens && y.out && x.p == y.p) ||
-                (x.p == pool && y.p == new_pool && x.p == y.p))
-                continue;
-            if (overlaps(x.p, x.n, y.p, y.n))
+    for (int x = kWant; x <= kStatus; ++x)
+        for (int y = x + 1; y <= kStatus; ++y) {
+            if (y < kTable || !parts[x].n || !parts[y].n) continue;     // two inputs, or nothing
+            // in place, and only these arrays (with want = lens nothing changes)
+            const bool twins = (x == kLens && y == kNewLens) || (x == kPool && y == kNewPool) ||
+                               (x == kWant && y == kNewLens && want == lens);
+            if (twins && parts[x].p == parts[y].p) continue;
+            if (overlaps(parts[x].p, parts[x].n, parts[y].p, parts[y].n))
                 return fail(QMM_EINVAL, "%s: an output overlaps another array", fn);
         }
     return finish(fn, qmm::launch_kv_plan({want, lens, table, ring, pool, new_lens, new_pool, cu,

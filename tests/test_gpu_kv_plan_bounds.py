@@ -103,3 +103,16 @@ def test_the_largest_number_of_rows(tokens):
     assert step.positions[:6].tolist() == [20, 21, 22, 23, 24, 0]
     for x in (step.slots, step.positions):
         assert len(x) == tokens and all((part == -1).all() for part in x[6:].split(1 << 28))
+
+
+def test_in_place_where_nothing_changes():
+    """want, lens and the new lens in one array."""
+    lens = torch.tensor([20, 0, 33], dtype=torch.int32, device="cuda")
+    table = torch.tensor([[7, 3, 0], [0, 0, 0], [1, 2, 4]], dtype=torch.int32, device="cuda")
+    ring, pool = torch.tensor([8, 9], dtype=torch.int32, device="cuda"), torch.tensor([1, 1], device="cuda")
+    before = table.clone()
+    out = qmm.KvPlan(lens, pool, torch.empty(4, dtype=torch.int32, device="cuda"),
+                     torch.empty(2, dtype=torch.int64, device="cuda"), None, torch.empty_like(lens))
+    qmm.kv_plan(lens, lens, table, ring, pool, 2, 16, out=out)
+    assert lens.tolist() == [20, 0, 33] and pool.tolist() == [1, 1] and torch.equal(table, before)
+    assert out.cu.tolist() == [0] * 4 and out.slots.tolist() == [-1, -1] and not out.status.any()

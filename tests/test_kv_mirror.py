@@ -37,6 +37,16 @@ def test_refusals():
                                0) == qmm.QMM_EALIGN
 
 
+@pytest.mark.parametrize("name", ["status", "cu", "positions", "slots", "table", "ring"])
+@pytest.mark.parametrize("twin", ["lens", "pool"])
+def test_a_plan_in_place_lets_no_other_output_share_the_array(name, twin):
+    names = ("want", "lens", "table", "ring", "pool", "new_lens", "new_pool", "cu", "slots", "positions", "status")
+    at = {n: (i + 1) << 40 for i, n in enumerate(names)}
+    at["new_" + twin] = at[name] = at[twin]
+    assert qmm.qmm_kv_plan(*at.values(), 3, 5, 4, 50, PAGE) == qmm.QMM_EINVAL
+    assert "overlaps" in qmm.qmm_last_error()
+
+
 @pytest.mark.gpu
 def test_the_same_as_the_front_ends():
     g = torch.Generator().manual_seed(3)
